@@ -323,6 +323,9 @@ __global__ void __launch_bounds__(32 * ap_warps(SELECTED), 1) k_weights_tiles(co
             if (!wait(&S.full[i], p / AP_RAW)) break;
             const ApProduct m = S.prod[d];
             if (m.flags & AP_STOP) {
+                // As with any half: before its place is free, a slower warp may have yet to
+                // arrive for the half that is there, and this arrival would count as its.
+                if (turn > 0 && !wait(&S.kfree[slot], turn - 1)) break;
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&S.kready[slot]);
                 break;
