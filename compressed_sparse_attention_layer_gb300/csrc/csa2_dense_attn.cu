@@ -32,6 +32,13 @@ static_assert(DN_KWARPS * DA_REGS + DA_SWARPS * DA_REGS_SOFTMAX + 4 * DA_REGS_IS
 // The weights of the value product are held between 2^DA_START (the largest, when
 // the reference is set) and 2^DA_PASS (when it has to move), inside f16's range.
 constexpr float DA_START = 0.0f, DA_PASS = 15.5f;
+// The sums' terms, 2^(logit - mu), lie between 2^-(Xk + 14) and 2^(16 - Xk) where they
+// count; times 2^DA_SUM that is inside fp32's range for every Xk from DN_XZERO to 127,
+// a million of them added up.  The factor is a part of the exponent once a segment has
+// had a scale above 2^DA_HIGH; otherwise it comes after, for the exponent would be
+// rounded at its size.
+constexpr float DA_SUM = 25.0f;
+constexpr int DA_HIGH = 64;
 // The tensor accumulator drops what is below its last place at every step, always
 // towards zero: over 1,048,576 entries of one row and values of one sign the output
 // came 0.65 % short, more than a step of bf16.  After every DA_FOLD tiles (1,024 steps)
@@ -40,8 +47,8 @@ constexpr float DA_START = 0.0f, DA_PASS = 15.5f;
 // 24.9 ms instead of 24.5.
 constexpr int DA_FOLD = 128;
 
-// A partial result: unnormalised output, running maximum (base 2) and sum per head; the
-// output of a segment's earlier tiles until it ends.
+// A partial result per head: unnormalised output and sum in units of 2^m, m = mu - DA_SUM;
+// the output of a segment's earlier tiles until it ends.
 struct DenseSlot {
     float o[CSA2_HEADS][CSA2_HEAD_DIM];
     float m[CSA2_HEADS], l[CSA2_HEADS];
@@ -79,6 +86,7 @@ struct DaSmem {
     float back[CSA2_HEADS];                        // 2^(held - mu): its factor
     float qe[2][CSA2_HEADS];                       // the query's 2^e_h (of the tile that brought it)
     float2 kv[2][DA_KEYS];                         // the keys of tile j in j % 2: (Xk, f), Xk = -inf for no key
+    uint8_t high[2][DN_KWARPS];                    // a key warp's Xk of tile j: one is above DA_HIGH
     uint32_t moved[2];                             // heads whose reference has just moved
     int64_t sums[DA_WARPS];
     int64_t total, g0;                             // tiles of all rows; the run's first
@@ -92,6 +100,13 @@ struct DaSmem {
     int abort;
     uint32_t tmem;
 };
+
+// log(L 2^M): L's own power of two goes to M's, for the two logarithms may cancel.
+__device__ __forceinline__ float dense_lse(float M, float L)
+{
+    const int k = min((int)(__float_as_uint(L) >> 23) - 127, 126);
+    return fmaf(M + (float)k, kLn2, logf(L * exp2i(-k)));
+}
 
 // Run i of `runs` equal ones takes the tiles from here up to dense_cut(i + 1).
 __device__ __forceinline__ int64_t dense_cut(int64_t total, int64_t runs, int64_t i) { return total * i / runs; }
@@ -122,7 +137,7 @@ __device__ __forceinline__ void dense_fold(uint32_t tmem, DenseSlot &slot, bool 
         tc::tmem_ld_wait(v);
 #pragma unroll
         for (int j = 0; j < 16; j++) {
-            const float x = __uint_as_float(v[j]) * exp2i(-(int)DN_XOFF);
+            const float x = __uint_as_float(v[j]) * exp2i((int)(DA_SUM - DN_XOFF));
             at[j * CSA2_HEAD_DIM] = first ? x : fmaf(at[j * CSA2_HEAD_DIM], S.back[h0 + j], x);
         }
     }
@@ -140,7 +155,7 @@ __device__ __forceinline__ void dense_output(uint32_t tmem, DenseSlot &slot, boo
     const int h = (int)threadIdx.x - 32 * DN_KWARPS;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     if (h < CSA2_HEADS) {
-        float L = (S.red[0][h] + S.red[1][h]) + (S.red[2][h] + S.red[3][h]), M = S.mu[h];
+        float L = (S.red[0][h] + S.red[1][h]) + (S.red[2][h] + S.red[3][h]), M = S.mu[h] - DA_SUM;
         if (part) {
             slot.m[h] = L > 0.0f ? M : -INFINITY;
             slot.l[h] = L;
@@ -157,7 +172,7 @@ __device__ __forceinline__ void dense_output(uint32_t tmem, DenseSlot &slot, boo
                 }
             }
             S.alpha[h] = L > 0.0f ? fct / L : 0.0f;
-            lse[h] = L > 0.0f ? fmaf(M, kLn2, logf(L)) : -INFINITY;
+            lse[h] = L > 0.0f ? dense_lse(M, L) : -INFINITY;
         }
     }
     tc::named_bar_sync(1, DA_STHREADS);
@@ -169,7 +184,7 @@ __device__ __forceinline__ void dense_output(uint32_t tmem, DenseSlot &slot, boo
         tc::tmem_ld16(tmem + lane_base + 64u * (uint32_t)mt + (uint32_t)h0, v);
         tc::tmem_ld_wait(v);
 #pragma unroll
-        for (int j = 0; j < 16; j++) v[j] = __float_as_uint(__uint_as_float(v[j]) * exp2i(-(int)DN_XOFF));
+        for (int j = 0; j < 16; j++) v[j] = __float_as_uint(__uint_as_float(v[j]) * exp2i((int)(DA_SUM - DN_XOFF)));
         if (__builtin_expect(folded, 0))
 #pragma unroll
             for (int j = 0; j < 16; j++) v[j] = __float_as_uint(fmaf(slot.o[h0 + j][dim], S.back[h0 + j], __uint_as_float(v[j])));
@@ -215,15 +230,18 @@ __device__ __forceinline__ void dense_query(const uint16_t *q, int r, int b, int
 __device__ __forceinline__ void dense_window_part(const csa2_swa &swa, const DenseRow &R, int b, int mt, int key, int lane)
 {
     DaSmem &S = dense_smem<DaSmem>();
+    bool high = false;
 #pragma unroll 1
     for (int h = 0; h < 2; h++) {
         const int64_t tok = R.lo + key + 64 * h;
         if (mt == 0) {
             const float2 v = dense_window_scale(swa, R, tok, lane);
             if ((lane & 3) == 0) S.kv[b][key + 64 * h] = v;
+            high = high || v.x > (float)DA_HIGH;
         }
         dense_store_window<DA_KSLAB>(S.k, swa, R, tok, mt, key + 64 * h, lane);
     }
+    if (mt == 0) S.high[b][key / DN_WKEYS] = __any_sync(0xffffffffu, high);
 }
 
 // Eight warps load and dequantise, eight take the softmax, one issues the products.
@@ -242,7 +260,8 @@ __device__ __forceinline__ void dense_window_part(const csa2_swa &swa, const Den
 //
 // The softmax works with y = logit (base 2) + Xk, the exponent of a key's weight
 // times its power of two: 2^(y - mu) is the f16 weight of the value product and
-// 2^(y - mu - Xk) the term of the sum.  The reference mu of a head is an integer,
+// 2^(y - mu - Xk + DA_SUM) the term of the sum (for a key of zeros, whose weight is 0, any Xk
+// will do: one that keeps the term finite).  The reference mu of a head is an integer,
 // set from the segment's first tile; weights down to 2^-14 of the largest keep
 // f16's 11 bits, smaller ones 2^-25 of it, and mu moves (the output then shrinks by
 // a power of two) only when a weight would pass 2^15.5, so most tiles need no
@@ -403,8 +422,9 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
                 bool zero;
                 xk[h] = dense_exponent<E4M3>(code[h], sc[h], &zero);
                 if (entries && (lane & 3) == 0)
-                    S.kv[b][key + 64 * h] = !there[h] ? make_float2(-INFINITY, 0.0f) : zero ? make_float2(0.0f, 0.0f) : make_float2((float)xk[h], 1.0f);
+                    S.kv[b][key + 64 * h] = !there[h] ? make_float2(-INFINITY, 0.0f) : zero ? make_float2(DN_XZERO, 0.0f) : make_float2((float)xk[h], 1.0f);
             }
+            if (entries) S.high[b][warp] = !E4M3 && __any_sync(0xffffffffu, max(xk[0], xk[1]) > DA_HIGH);
             bool ok = true;
 #pragma unroll
             for (int mt = 0; mt < DA_PARTS; mt++) {
@@ -443,6 +463,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
         int r = S.row0, ti = S.ti0, tiles = dense_row(bt, evicted, swa, r).tiles;
         bool owned = ti == 0;                      // this run holds the row's first tile
         bool seen = false;                         // the segment has had a key with a weight
+        bool high = false;                         // ... one of a scale above 2^DA_HIGH
         float a[8], mu[8], l[8];                   // per head: factor of a product, reference, sum
         for (int j = 0; j < n; j++) {
             const uint32_t b = j & 1, ph = j & 1;
@@ -450,17 +471,16 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
             // the keys' part of the arithmetic, while the logits are on their way
             bool ok = dense_wait(&S.kbar[0], ph, &S.abort, polls, c.status);
             if (__builtin_expect(first, 0)) {
-                seen = false;
+                seen = high = false;
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
                     a[i] = S.qe[b][hd + 8 * (i >> 1) + (i & 1)] * scale;
                     mu[i] = l[i] = 0.0f;
                 }
             }
-            // Of each key: its exponent, the factor of its products, 2^-Xk, and f.  A key of
-            // zeros has no weight in the value product and moves the reference only so far
-            // that its term of the sum, 2^-mu, stays finite (shift).
-            float kx[4], kf[4], ix[4], ky[4], shift[4];
+            // Of each key: its exponent, the factor of its products, and f.
+            float kx[4], kf[4], ky[4];
+            high = high || *reinterpret_cast<const uint64_t *>(S.high[b]) != 0;
 #pragma unroll
             for (int u = 0; u < 4; u++) {
                 const float2 kv = S.kv[b][key + 8 * u];
@@ -469,8 +489,6 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
                 kx[u] = kv.x;
                 ky[u] = kv.y;
                 kf[u] = none ? 0.0f : exp2i(xi - (int)DN_XOFF) * kv.y;
-                ix[u] = none ? 0.0f : exp2i(max(-xi, -126));
-                shift[u] = kv.y == 0.0f ? 100.0f : 0.0f;
             }
             ok = dense_wait(&S.sbar, ph, &S.abort, polls, c.status) && ok;
             tc::tc_fence_after();
@@ -481,7 +499,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
                 uint32_t v[16];
                 tmem_ld_16x32(tmem + DA_S_COL + lane_base + ((uint32_t)(16 * w) << 16) + (uint32_t)h32, v);
                 tc::tmem_ld_wait(v);
-                float top[2] = {-INFINITY, -INFINITY};
+                float top = -INFINITY;
 #pragma unroll
                 for (int at = 0; at < 16; at += 2) {
                     const int u = (at >> 1) & 1, i = 2 * (at >> 2), k = 2 * w + u;
@@ -490,9 +508,9 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
                                                f32x2_sub(make_float2(kx[k], kx[k]), make_float2(mu[i], mu[i + 1])));
                     x[16 * w + at] = y.x;
                     x[16 * w + at + 1] = y.y;
-                    top[u] = fmaxf(top[u], fmaxf(y.x, y.y));
+                    top = fmaxf(top, fmaxf(y.x, y.y));
                 }
-                pass = pass || top[0] - shift[2 * w] > DA_PASS || top[1] - shift[2 * w + 1] > DA_PASS;
+                pass = pass || top > DA_PASS;
             }
             if (__builtin_expect(named_bar_or(1, DA_STHREADS, pass || !ok), 0)) {
                 // the earlier value products are done before their output shrinks
@@ -503,7 +521,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
                     const int at = 4 * (i >> 1) + (i & 1);
-                    mx[i] = fmaxf(fmaxf(x[at] - shift[0], x[at + 2] - shift[1]), fmaxf(x[at + 16] - shift[2], x[at + 18] - shift[3]));
+                    mx[i] = fmaxf(fmaxf(x[at], x[at + 2]), fmaxf(x[at + 16], x[at + 18]));
 #pragma unroll
                     for (int w = 4; w < 32; w <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], w));
                     if (lane < 4) S.red[quarter][hd + 8 * (i >> 1) + (i & 1)] = mx[i];
@@ -556,12 +574,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
                         const int at = 16 * (u >> 1) + 4 * i + 2 * (u & 1);
-                        const float2 e = make_float2(exp2_approx(x[at]), exp2_approx(x[at + 1]));
-                        const float2 sum = f32x2_fma(e, make_float2(ix[u], ix[u]), make_float2(l[2 * i], l[2 * i + 1]));
-                        l[2 * i] = sum.x;
-                        l[2 * i + 1] = sum.y;
-                        // the weights' rounding to f16 (2^-11); their sum takes the fp32 value
-                        const float2 wt = f32x2_mul(e, make_float2(ky[u], ky[u]));
+                        // the weights' rounding to f16 (2^-11); their sum takes fp32 values
+                        const float2 wt = f32x2_mul(make_float2(exp2_approx(x[at]), exp2_approx(x[at + 1])), make_float2(ky[u], ky[u]));
                         uint32_t pk;
                         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk) : "f"(wt.y), "f"(wt.x));
                         *reinterpret_cast<uint32_t *>(row + ((((uint32_t)h32 >> 3) + i ^ ((uint32_t)key & 7u)) << 4)) = pk;
@@ -572,6 +586,21 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&S.pbar);
+            // The sums, while the value product runs: 2^(y - mu - Xk) by an exponential of its own,
+            // for 2^(y - mu) may be below fp32's range where the term is not.
+            const float off = high ? DA_SUM : E4M3 ? DN_XOFF : 0.0f, fct = exp2i((int)(DA_SUM - off));
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                const float xk = kx[u] == -INFINITY ? 0.0f : kx[u] - off;
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const int k = 16 * (u >> 1) + 2 * i + 2 * (u & 1);
+                    const float2 y = f32x2_sub(make_float2(x[k], x[k + 1]), make_float2(xk, xk));
+                    const float2 sum = f32x2_fma(make_float2(exp2_approx(y.x), exp2_approx(y.y)), make_float2(fct, fct), make_float2(l[i], l[i + 1]));
+                    l[i] = sum.x;
+                    l[i + 1] = sum.y;
+                }
+            }
             const int at = min(j, ti);             // the tile's place in its segment
             // a segment's slot: a row that a run begins in its middle (or with) is the
             // run's first, any other its second
@@ -669,7 +698,7 @@ __global__ void __launch_bounds__(DM_THREADS)
         if (sink) L += exp2f(z - base);
         const float inv = L > 0.0f ? 1.0f / L : 0.0f;
         for (int i = lane; i < parts; i += 32) wgt[i][j] *= inv;
-        if (lane == 0) lse[r * CSA2_HEADS + h] = L > 0.0f ? fmaf(M, kLn2, logf(L)) : -INFINITY;
+        if (lane == 0) lse[r * CSA2_HEADS + h] = L > 0.0f ? dense_lse(M, L) : -INFINITY;
     }
     __syncthreads();
     // a thread's eight dims of one head

@@ -13,7 +13,7 @@
 //          (every product of a code and a scale is an f16); for a window row Xk
 //          - 12 and f are the exponent and the mantissa (at most 1) of its scale,
 //          K' its codes.  A key of zeros has no exponent: its logit is 0 and it adds
-//          nothing to the output, (Xk, f) = (0, 0);
+//          nothing to the output, (Xk, f) = (DN_XZERO, 0);
 //   query  q_h = Q'_h 2^e_h with the head's largest element in [2^13, 2^14):
 //          elements down to 2^-27 of it keep their bf16 value.
 #pragma once
@@ -31,8 +31,10 @@ constexpr uint32_t DN_KBYTES = DN_SLABS * DN_KSLAB, DN_QBYTES = DN_SLABS * CSA2_
 constexpr uint32_t DN_QSLAB = CSA2_HEADS * 128;    // bytes of a slab of the query operand
 
 constexpr float DN_XOFF = 12.0f;                   // K' is the key times 2^(DN_XOFF - Xk)
-// Smallest Xk: the sums of weights divided by 2^Xk stay finite.
-constexpr int DN_XMIN = -90;
+// Smallest Xk: the sums of weights divided by 2^Xk stay finite.  (The codes of a block of
+// scale 2^-101 are still exact.)
+constexpr int DN_XMIN = -66;
+constexpr float DN_XZERO = -68.0f;                 // a key of zeros: below the others, which set the reference
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
 // What query row r attends to.
@@ -225,7 +227,7 @@ __device__ __forceinline__ void dense_store_window(uint8_t *ktile, const csa2_sw
 }
 
 // (Xk, f) of the window row that a quad of lanes holds; (-inf, 0) where there is
-// no row.  The quantiser gives a row of zeros the scale 1, which may be far above
+// no row, (DN_XZERO, 0) for one of zeros.  The quantiser gives a row of zeros the scale 1, which may be far above
 // its neighbours': such a row is told by its codes.  Called by the whole warp.
 __device__ __forceinline__ float2 dense_window_scale(const csa2_swa &swa, const DenseRow &R, int64_t tok, int lane)
 {
@@ -248,8 +250,8 @@ __device__ __forceinline__ float2 dense_window_scale(const csa2_swa &swa, const 
         zero = zero || any == 0;
     }
     if (!row) return make_float2(-INFINITY, 0.0f);
-    if (zero) return make_float2(0.0f, 0.0f);
-    const int e = max((int)((__float_as_uint(s) >> 23) & 255u) - 126, DN_XMIN);    // |f| <= 1
+    if (zero) return make_float2(DN_XZERO, 0.0f);
+    const int e = max((int)((__float_as_uint(s) >> 23) & 255u) - 126, DN_XMIN - (int)DN_XOFF);    // |f| <= 1
     return make_float2((float)e + DN_XOFF, s * exp2i(-min(e, 126)));
 }
 

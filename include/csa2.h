@@ -453,7 +453,7 @@ CSA2_API int csa2_sparse_attn_schedule(const csa2_batch *batch, const csa2_swa *
  * Logits, references, sums and outputs are held in fp32.  The query is carried in
  * f16 with a power of two per head (exact down to 2^-27 of the head's largest
  * element, to 2^-38 of it below), the keys exactly but for MXFP4 blocks 2^36
- * below their entry's largest.  The weights of the value product are f16
+ * below their entry's largest or of scales below 2^-101.  The weights of the value product are f16
  * (2^-11), with a power of two per key (its largest block scale) and per head:
  * one whose product with its key's scale is below 2^-25 of the largest adds
  * nothing to o; the sum takes every weight in fp32.  A page id outside the cache

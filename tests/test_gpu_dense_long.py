@@ -34,3 +34,30 @@ def test_positive_values_of_a_long_sequence(fmt, B, n):
     d = case.cuda()
     case.check(d, sorted({0, 1 % B, B // 2, B - 1}), 4e-4)
     assert int(d.status) == 0 and bool(torch.isfinite(d.o).all())
+
+
+@pytest.mark.parametrize("low,high", [(-70, 60), (-40, 60), (-85, 45), (0, 127), (-90, -89), (-60, 100)])
+def test_scales_far_apart(low, high):
+    """Entries of scale 2^high among entries of 2^low, a query of zeros: every entry has
+    the same weight, whatever its scale.  lse = log n, o = the mean."""
+    rng = np.random.default_rng(high - low)
+    n = 130
+    nib = rng.integers(1, 5, (192, 512)) | rng.integers(0, 2, (192, 512)) << 3
+    scales = np.repeat(np.where(np.arange(192) % 2, low, high)[:, None] + 127, 16, 1).astype(np.uint8)
+    nib[7] = 0                                     # and one of zeros
+    case = LongCase(codes_of(nib), scales, np.arange(3)[None].repeat(2, 0), [n, 1], np.zeros((2, HEADS, 512), np.float32))
+    d = case.cuda()
+    e = case.keys[:n].mean(0)
+    lse = d.lse.cpu().numpy()
+    # lse = mu ln 2 + log(sum / 2^mu) with |mu| <= 128: two terms of up to 89 that cancel, ln 2 rounded
+    # (2^-24 of 89), the logarithm (2^-23 of it) and the result (2^-24): 4 x 2^-24 x 89 < 2^-15
+    assert np.abs(lse[0] - np.log(n)).max() <= 2.0 ** -15 and np.abs(lse[1]).max() <= 2.0 ** -15
+    # (equal weights are one power of two in f16)
+    o = d.o.float().cpu().numpy().astype(np.float64)
+    size = np.abs(case.keys[:n]).mean(0)
+    assert (np.abs(o[0] - e) <= 2.0 ** -8 * np.abs(e) + 2.0 ** -14 * size).all()
+    # (a single entry is its own output; 2.0 x 2^127 lies beyond fp32 and bf16)
+    one = np.where(np.abs(case.keys[0]) < 2.0 ** 128, case.keys[0], np.sign(case.keys[0]) * np.inf)
+    finite = np.isfinite(one)
+    assert (np.abs(o[1] - one)[:, finite] <= 2.0 ** -8 * np.abs(one[finite])).all()
+    assert (o[1][:, ~finite] == one[~finite]).all()
