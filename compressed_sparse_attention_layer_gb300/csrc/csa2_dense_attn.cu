@@ -30,8 +30,15 @@ static_assert(DN_KWARPS * DA_REGS + DA_SWARPS * DA_REGS_SOFTMAX + 4 * DA_REGS_IS
                   DA_THREADS * DA_REGS <= 65536,
               "the launch's registers");
 // The weights of the value product are held between 2^DA_START (the largest, when
-// the reference is set) and 2^DA_PASS (when it has to move), inside f16's range.
-constexpr float DA_START = 0.0f, DA_PASS = 15.5f;
+// the reference is set) and 2^DA_PASS (when it has to move), inside f16's range.  One
+// below 2^-25 adds nothing to the output, while the sum has it: up to 2^-24 of the
+// largest for each entry.  A long rest far below one entry must not go missing like
+// that, so when a segment has had DA_FOLD tiles its references go down by up to 8, and a
+// later move ends at DA_LATE: n entries lose at most min(n, 16384) 2^-24 + n 2^-32 of the
+// largest, 2^-9.7 for a million.  (Without it 2.5 % of the mass were missing behind a first
+// entry that stood 17.5 above 1,048,575 others.)  DA_LATE from the start costs moves: 64 x
+// 32,768 entries take 449 us, from the 32nd tile on 432, from the 64th 417, from the 128th 408.
+constexpr float DA_START = 0.0f, DA_LATE = 8.0f, DA_PASS = 15.5f;
 // The sums' terms, 2^(logit - mu), lie between 2^-(Xk + 14) and 2^(16 - Xk) where they
 // count; times 2^DA_SUM that is inside fp32's range for every Xk from DN_XZERO to 127,
 // a million of them added up.  The factor is a part of the exponent once a segment has
@@ -86,7 +93,7 @@ struct DaSmem {
     float back[CSA2_HEADS];                        // 2^(held - mu): its factor
     float qe[2][CSA2_HEADS];                       // the query's 2^e_h (of the tile that brought it)
     float2 kv[2][DA_KEYS];                         // the keys of tile j in j % 2: (Xk, f), Xk = -inf for no key
-    uint8_t high[2][DN_KWARPS];                    // a key warp's Xk of tile j: one is above DA_HIGH
+    int8_t xtop[2][DN_KWARPS];                     // a key warp's largest Xk of the segment up to tile j (at most 127)
     uint32_t moved[2];                             // heads whose reference has just moved
     int64_t sums[DA_WARPS];
     int64_t total, g0;                             // tiles of all rows; the run's first
@@ -227,21 +234,23 @@ __device__ __forceinline__ void dense_query(const uint16_t *q, int r, int b, int
 }
 
 // Part mt of a row's window tile (no rows behind the last, or for a row without one).
-__device__ __forceinline__ void dense_window_part(const csa2_swa &swa, const DenseRow &R, int b, int mt, int key, int lane)
+// xtop: the segment's largest Xk before.
+__device__ __forceinline__ void dense_window_part(const csa2_swa &swa, const DenseRow &R, int b, int mt, int key, int lane,
+                                                  int xtop)
 {
     DaSmem &S = dense_smem<DaSmem>();
-    bool high = false;
+    float top = -INFINITY;
 #pragma unroll 1
     for (int h = 0; h < 2; h++) {
         const int64_t tok = R.lo + key + 64 * h;
         if (mt == 0) {
             const float2 v = dense_window_scale(swa, R, tok, lane);
             if ((lane & 3) == 0) S.kv[b][key + 64 * h] = v;
-            high = high || v.x > (float)DA_HIGH;
+            top = fmaxf(top, v.x);
         }
         dense_store_window<DA_KSLAB>(S.k, swa, R, tok, mt, key + 64 * h, lane);
     }
-    if (mt == 0) S.high[b][key / DN_WKEYS] = __any_sync(0xffffffffu, high);
+    if (mt == 0) S.xtop[b][key / DN_WKEYS] = (int8_t)max(xtop, __reduce_max_sync(0xffffffffu, (int)fminf(fmaxf(top, DN_XZERO), 127.0f)));
 }
 
 // Eight warps load and dequantise, eight take the softmax, one issues the products.
@@ -263,7 +272,7 @@ __device__ __forceinline__ void dense_window_part(const csa2_swa &swa, const Den
 // 2^(y - mu - Xk + DA_SUM) the term of the sum (for a key of zeros, whose weight is 0, any Xk
 // will do: one that keeps the term finite).  The reference mu of a head is an integer,
 // set from the segment's first tile; weights down to 2^-14 of the largest keep
-// f16's 11 bits, smaller ones 2^-25 of it, and mu moves (the output then shrinks by
+// f16's 11 bits, smaller ones 2^-24 of it (2^-22 and 2^-32 after the first fold), and mu moves (the output then shrinks by
 // a power of two) only when a weight would pass 2^15.5, so most tiles need no
 // maximum across lanes, only one barrier that says that nothing passed.
 template <bool E4M3>
@@ -382,7 +391,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
     } else if (warp < DN_KWARPS) {
         // ================================================ the keys
         const int key = DN_WKEYS * warp + (lane >> 2);          // this quad's keys: key and key + 64
-        int r = S.row0, ti = S.ti0;
+        int r = S.row0, ti = S.ti0, xtop = 0;
         DenseRow R = dense_row(bt, evicted, swa, r);
         auto wait = [&](uint64_t *bar, int phase) { return dense_wait(bar, phase & 1, &S.abort, polls, c.status); };
         // The next tile's codes, on their way while this one is in its softmax (loads are
@@ -424,7 +433,11 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
                 if (entries && (lane & 3) == 0)
                     S.kv[b][key + 64 * h] = !there[h] ? make_float2(-INFINITY, 0.0f) : zero ? make_float2(DN_XZERO, 0.0f) : make_float2((float)xk[h], 1.0f);
             }
-            if (entries) S.high[b][warp] = !E4M3 && __any_sync(0xffffffffu, max(xk[0], xk[1]) > DA_HIGH);
+            if (j == 0 || ti == 0) xtop = (int)DN_XZERO;
+            if (entries) {
+                xtop = max(xtop, E4M3 ? xk[0] : __reduce_max_sync(0xffffffffu, min(max(xk[0], xk[1]), 127)));
+                S.xtop[b][warp] = (int8_t)xtop;
+            }
             bool ok = true;
 #pragma unroll
             for (int mt = 0; mt < DA_PARTS; mt++) {
@@ -436,7 +449,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
                     for (int h = 0; h < 2; h++)
                         dense_store<E4M3, DA_KSLAB>(S.k, code[h][mt], sc[h], xk[h], there[h], mt, mt, key + 64 * h, lane);
                 } else {
-                    dense_window_part(swa, R, b, mt, key, lane);
+                    dense_window_part(swa, R, b, mt, key, lane, xtop);
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp();
@@ -463,7 +476,6 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
         int r = S.row0, ti = S.ti0, tiles = dense_row(bt, evicted, swa, r).tiles;
         bool owned = ti == 0;                      // this run holds the row's first tile
         bool seen = false;                         // the segment has had a key with a weight
-        bool high = false;                         // ... one of a scale above 2^DA_HIGH
         float a[8], mu[8], l[8];                   // per head: factor of a product, reference, sum
         for (int j = 0; j < n; j++) {
             const uint32_t b = j & 1, ph = j & 1;
@@ -471,7 +483,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
             // the keys' part of the arithmetic, while the logits are on their way
             bool ok = dense_wait(&S.kbar[0], ph, &S.abort, polls, c.status);
             if (__builtin_expect(first, 0)) {
-                seen = high = false;
+                seen = false;
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
                     a[i] = S.qe[b][hd + 8 * (i >> 1) + (i & 1)] * scale;
@@ -479,8 +491,11 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
                 }
             }
             // Of each key: its exponent, the factor of its products, and f.
+            const int at = min(j, ti);             // the tile's place in its segment
             float kx[4], kf[4], ky[4];
-            high = high || *reinterpret_cast<const uint64_t *>(S.high[b]) != 0;
+            const uint2 xt = *reinterpret_cast<const uint2 *>(S.xtop[b]);       // eight bytes
+            const uint32_t xt4 = __vmaxs4(xt.x, xt.y);
+            const bool high = __vcmpgts4(xt4, 0x01010101u * DA_HIGH) != 0;
 #pragma unroll
             for (int u = 0; u < 4; u++) {
                 const float2 kv = S.kv[b][key + 8 * u];
@@ -534,8 +549,9 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
                     const float m = fmaxf(fmaxf(S.red[0][h], S.red[1][h]), fmaxf(S.red[2][h], S.red[3][h]));
                     // (with the head that passed move all that have come near: 400 us, with
                     // those above 2^7.5 alone 409, for there are fewer moves to come)
-                    const bool up = seen ? m > DA_PASS - 14.0f : m > -INFINITY;
-                    const float d = up ? ceilf(m) - DA_START : 0.0f;
+                    const float start = seen && at >= DA_FOLD ? DA_LATE : DA_START;
+                    const bool up = seen ? m > start + 1.5f : m > -INFINITY;
+                    const float d = up ? ceilf(m) - start : 0.0f;
                     const float f = exp2_approx(fminf(-d, 120.0f));             // (more only for sums of nothing)
                     mx[i] = m;
                     mu[i] += d;
@@ -574,7 +590,9 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
                         const int at = 16 * (u >> 1) + 4 * i + 2 * (u & 1);
-                        // the weights' rounding to f16 (2^-11); their sum takes fp32 values
+                        // the weights' rounding to f16 (2^-11, an eighth of the output's to bf16; a second
+                        // f16 for the rest would be as much value product again, 1,536 cycles a tile, and
+                        // 16 KB that are not there); their sum takes fp32 values
                         const float2 wt = f32x2_mul(make_float2(exp2_approx(x[at]), exp2_approx(x[at + 1])), make_float2(ky[u], ky[u]));
                         uint32_t pk;
                         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk) : "f"(wt.y), "f"(wt.x));
@@ -601,7 +619,6 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
                     l[i + 1] = sum.y;
                 }
             }
-            const int at = min(j, ti);             // the tile's place in its segment
             // a segment's slot: a row that a run begins in its middle (or with) is the
             // run's first, any other its second
             DenseSlot &slot = slots[2 * blockIdx.x + (j > ti ? 1 : 0)];
@@ -610,26 +627,21 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
                 tc::tc_fence_after();
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
-                    const int h = hd + 8 * (i >> 1) + (i & 1);
-                    if (quarter == 0 && lane < 4) {
-                        if (at >= DA_FOLD) S.back[h] = exp2_approx(fminf(S.held[h] - mu[i], 120.0f));    // (more only for nothing)
-                        S.held[h] = mu[i];
-                    }
-                }
-            }
-            if (__builtin_expect(last, 0)) {
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
                     float v = l[i];
 #pragma unroll
                     for (int w = 4; w < 32; w <<= 1) v += __shfl_xor_sync(0xffffffffu, v, w);
                     const int h = hd + 8 * (i >> 1) + (i & 1);
                     if (lane < 4) {
                         S.red[quarter][h] = v;
-                        if (quarter == 0) S.mu[h] = mu[i];
+                        if (quarter == 0) {
+                            S.back[h] = exp2_approx(fminf(S.held[h] - mu[i], 120.0f));      // (more only for nothing)
+                            S.held[h] = S.mu[h] = mu[i];
+                        }
                     }
                 }
                 if (named_bar_or(1, DA_STHREADS, !ok)) break;
+            }
+            if (__builtin_expect(last, 0)) {
                 const bool whole = ti == tiles - 1 && owned;
                 if (sw == 0 && lane == 0 && !whole && owned)
                     dense_head(heads, r, (int)(&slot - slots), S.g0 + j - ti + tiles - 1, S.total);
@@ -637,9 +649,22 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
                              lse + (int64_t)r * CSA2_HEADS, swa.sink, swa.rope_base > 0.0f, bt.q_pos + r, turns);
                 tc::tc_fence_before();
             } else if (__builtin_expect((at + 1) % DA_FOLD == 0, 0)) {
-                if (named_bar_or(1, DA_STHREADS, !ok)) break;
                 dense_fold(tmem, slot, at < DA_FOLD);
                 tc::tc_fence_before();
+                if (at < DA_FOLD) {
+                    // The references go down for the rest, as far as the largest weight so far --
+                    // at most 2^Xk of the sum -- stays below 2^13.
+                    const int x = max(max((int8_t)xt4, (int8_t)(xt4 >> 8)), max((int8_t)(xt4 >> 16), (int8_t)(xt4 >> 24)));
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const int h = hd + 8 * (i >> 1) + (i & 1);
+                        const float L = (S.red[0][h] + S.red[1][h]) + (S.red[2][h] + S.red[3][h]);
+                        const int top = (int)(__float_as_uint(L) >> 23) - 126 - (int)DA_SUM + x;
+                        const int down = L > 0.0f ? min(max(13 - top, 0), (int)(DA_LATE - DA_START)) : 0;
+                        mu[i] -= (float)down;
+                        l[i] *= exp2i(down);
+                    }
+                }
             }
             if (__builtin_expect(++ti == tiles && j + 1 < n, 0)) {
                 ti = 0;

@@ -453,11 +453,13 @@ CSA2_API int csa2_sparse_attn_schedule(const csa2_batch *batch, const csa2_swa *
  * Logits, references, sums and outputs are held in fp32.  The query is carried in
  * f16 with a power of two per head (exact down to 2^-27 of the head's largest
  * element, to 2^-38 of it below), the keys exactly but for MXFP4 blocks 2^36
- * below their entry's largest or of scales below 2^-101.  The weights of the value product are f16
- * (2^-11), with a power of two per key (its largest block scale) and per head:
- * one whose product with its key's scale is below 2^-25 of the largest adds
- * nothing to o; the sum takes every weight in fp32.  A page id outside the cache
- * holds no keys (CSA2_DEV_BAD_PAGE). */
+ * below their entry's largest or of scales below 2^-101.  The weights of the value
+ * product are f16 (2^-11, an eighth of the output's own rounding), with a power of
+ * two per key (its largest block scale) and per head: of one whose product with its
+ * key's scale is below 2^-24 of the largest nothing may reach o, 2^-32 behind the
+ * first 16,384 entries of a run, so n entries lose at most min(n, 16384) 2^-24 +
+ * n 2^-32 of the largest; the sum takes every weight in fp32.  A page id outside the
+ * cache holds no keys (CSA2_DEV_BAD_PAGE). */
 CSA2_API int csa2_dense_attn(const csa2_cache *cache, const csa2_batch *batch, const int64_t *evicted,
                              const uint16_t *q, float sm_scale, const csa2_swa *swa, uint16_t *o, float *lse,
                              void *workspace, size_t workspace_bytes, csa2_stream_t stream);

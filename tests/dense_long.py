@@ -47,14 +47,16 @@ class LongCase:
 
     def bounds(self, b, dl):
         """Of o and lse, dl bounding a logit's error: o is rounded to bf16 (2^-8), a weight to f16 (2^-11)
-        with a floor of half of f16's smallest step, 2^-25, where the largest is 2^7 or more (2^-32 of the
-        largest p w, w = 2^Xk; key j takes k_j / w_j times it); 1,024 steps of the accumulator, each with 17
+        with a floor of half of f16's smallest step, 2^-25, where the largest is 2^-1 or more for the first
+        16,384 entries of each of a row's segments (152 runs cut the rows), 2^7 or more behind them (2^-24 and 2^-32
+        of the largest p w, w = 2^Xk; key j takes k_j / w_j times it); 1,024 steps of the accumulator, each with 17
         addends that lose at most 2^-23 of the sum so far, half of the whole on average; twice the logits'
         error and 2^-20 for the exponentials and their sum."""
         o, lse, size, p = self.attention(b)
         t = self.times(b)
         one = np.where(t > 0, p / np.maximum(t, 1), 0.0)                       # a single entry's weight
-        floor = 2.0 ** -32 * (one * self.unit).max(1)[:, None] * (t[:, None] * np.abs(self.keys) / self.unit[:, None]).sum(0)[None]
+        small = (2.0 ** -24 * min(self.n[b], (152 // len(self.n) + 3) * 16384) + 2.0 ** -32 * self.n[b]) / self.n[b]
+        floor = small * (one * self.unit).max(1)[:, None] * (t[:, None] * np.abs(self.keys) / self.unit[:, None]).sum(0)[None]
         tol_o = 2.0 ** -8 * np.abs(o) + (2.0 ** -11 + 1024 * 17 * 2.0 ** -24 + 2 * dl + 2.0 ** -20) * size + floor
         return o, lse, tol_o, dl + 2.0 ** -16 + 2.0 ** -20 * np.abs(lse)
 

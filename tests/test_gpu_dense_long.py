@@ -61,3 +61,25 @@ def test_scales_far_apart(low, high):
     finite = np.isfinite(one)
     assert (np.abs(o[1] - one)[:, finite] <= 2.0 ** -8 * np.abs(one[finite])).all()
     assert (o[1][:, ~finite] == one[~finite]).all()
+
+
+@pytest.mark.parametrize("B,n,nats", [(152, 1 << 17, 17.5), (152, 1 << 20, 17.5), (152, 1 << 20, 16.2), (157, 1 << 18, 19.0),
+                                      (152, 1 << 20, 0.3)])
+def test_one_entry_above_a_long_rest(B, n, nats):
+    """The first entry stands `nats` above all others, which share a mean: together they are up to a tenth
+    of the weight, each 2^-23 to 2^-27 of the first's.  A logit is a sum of 64 like terms and smaller ones:
+    32 steps lose at most 17 x 2^-23 of 1.2 nats each."""
+    rng = np.random.default_rng(int(nats * 10) + n)
+    nib = rng.integers(0, 16, (65 * 64, 512))
+    nib[:, :64] = 2                                # 1.0 where the query looks
+    nib[:, 256:] = rng.integers(4, 8, (65 * 64, 256))
+    nib[0, :64] = 7                                # 6.0
+    nib[0, 256:] = 11                              # -1.5
+    table = repeated_pages(B, n // 64, 64, first=1)
+    table[:, 0] = 0
+    q = np.zeros((B, HEADS, 512), np.float32)
+    q[..., :64] = nats / 5 / 64
+    q[..., 64:256] = 0.002 * rng.standard_normal((B, HEADS, 192))
+    case = LongCase(codes_of(nib), np.full((65 * 64, 16), 127, np.uint8), table, [n] * B, bf16_values(q))
+    d = case.cuda()
+    case.check(d, [0, B // 2, B - 1], 32 * 17 * 2.0 ** -23 * 1.2 * nats)
