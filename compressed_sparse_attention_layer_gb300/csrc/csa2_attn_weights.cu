@@ -422,7 +422,9 @@ __global__ void __launch_bounds__(32 * ap_warps(SELECTED), 1) k_weights_tiles(co
                     if (key + 8 * u < m.lim) a.acc[m.b * a.ld + e[u]] += s[u];
                 } else if (e[u] >= 0) {
                     // the same entry twice in a row has the same weight: the order of its sums does not matter
-                    if (a.fix) atomicAdd(a.fix + (int64_t)m.b * a.bt.max_entries + e[u], (unsigned long long)(fminf(s[u], 64.0f) * AW_FIX));
+                    // (NaN has no fixed point: it goes to acc, which then stays NaN)
+                    if (a.fix && s[u] != s[u]) a.acc[(int64_t)m.b * a.ld + e[u]] = NAN;
+                    else if (a.fix) atomicAdd(a.fix + (int64_t)m.b * a.bt.max_entries + e[u], (unsigned long long)(fminf(s[u], 64.0f) * AW_FIX));
                     else atomicAdd(a.acc + (int64_t)m.b * a.ld + e[u], s[u]);
                 }
             }

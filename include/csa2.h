@@ -490,7 +490,8 @@ CSA2_API size_t csa2_dense_attn_workspace_size(const csa2_batch *batch);
  * as by csa2_dense_attn; exponentials and sums are fp32.
  * The same inputs give the same bits: an entry's sum is taken in a fixed order,
  * over the rows of a selecting call with nq > 1 in 64-bit fixed point (steps of
- * 2^-40, a row's weight of an entry taken as at most 64). */
+ * 2^-40, a row's weight of an entry taken as at most 64).  A NaN makes the entries
+ * that its query gives weight to NaN. */
 CSA2_API int csa2_attn_weights(const csa2_cache *cache, const csa2_batch *batch, const int64_t *evicted,
                                const uint16_t *q, float sm_scale, const int32_t *idx, int32_t k, const csa2_swa *swa,
                                const float *lse, float *acc, int64_t ld, void *workspace, size_t workspace_bytes,
