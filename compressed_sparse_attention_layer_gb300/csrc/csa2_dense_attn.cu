@@ -164,7 +164,7 @@ __device__ __forceinline__ void dense_output(uint32_t tmem, DenseSlot &slot, boo
     if (h < CSA2_HEADS) {
         float L = (S.red[0][h] + S.red[1][h]) + (S.red[2][h] + S.red[3][h]), M = S.mu[h] - DA_SUM;
         if (part) {
-            slot.m[h] = L > 0.0f ? M : -INFINITY;
+            slot.m[h] = L == 0.0f ? -INFINITY : M;
             slot.l[h] = L;
         } else {
             float fct = 1.0f;
@@ -178,8 +178,8 @@ __device__ __forceinline__ void dense_output(uint32_t tmem, DenseSlot &slot, boo
                     L += exp2f(z - M);
                 }
             }
-            S.alpha[h] = L > 0.0f ? fct / L : 0.0f;
-            lse[h] = L > 0.0f ? dense_lse(M, L) : -INFINITY;
+            S.alpha[h] = L == 0.0f ? 0.0f : fct / L;               // (NaN stays NaN)
+            lse[h] = L == 0.0f ? -INFINITY : dense_lse(M, L);
         }
     }
     tc::named_bar_sync(1, DA_STHREADS);
@@ -721,9 +721,9 @@ __global__ void __launch_bounds__(DM_THREADS)
 #pragma unroll
         for (int w = 1; w < 32; w <<= 1) L += __shfl_xor_sync(0xffffffffu, L, w);
         if (sink) L += exp2f(z - base);
-        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
         for (int i = lane; i < parts; i += 32) wgt[i][j] *= inv;
-        if (lane == 0) lse[r * CSA2_HEADS + h] = L > 0.0f ? dense_lse(M, L) : -INFINITY;
+        if (lane == 0) lse[r * CSA2_HEADS + h] = L == 0.0f ? -INFINITY : dense_lse(M, L);
     }
     __syncthreads();
     // a thread's eight dims of one head

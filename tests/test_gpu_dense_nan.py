@@ -38,3 +38,21 @@ def test_weights_of_a_poisoned_query_are_nan(nq, selected):
     sees[0, idx[bad][idx[bad] >= 0] if selected else case.entries(0, nq - 1)] = True
     assert np.array_equal(np.isnan(got), sees)
     assert (np.abs(got - want)[~sees] <= tol[~sees]).all() and int(d.status) == 0
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("lens,nq", [([300], 1), ([9000, 130], 1), ([700], 3)])
+def test_a_poisoned_head_is_nan_and_the_others_are_right(lens, nq, bad):
+    """Whole rows, rows cut into parts, several queries.  Logits that fall by hundreds from the first entries
+    on, so that a reference that followed them down would leave the range."""
+    case = DenseCase(83, lens, nq=nq, q_scale=40.0, window=len(lens) == 2)
+    d = case.cuda()
+    heads = [0, 9, 33]
+    d.q[0, heads, 200] = bad
+    csa2.csa2_dense_attn(d.cache, d.batch, d.q, case.sm_scale, d.o, d.lse, swa=d.swa)
+    o, lse = d.o.float().cpu().numpy(), d.lse.cpu().numpy()
+    assert np.isnan(lse[0, heads]).all() and np.isnan(o[0, heads]).all()
+    rest = [h for h in range(64) if h not in heads]
+    eo, el, to, tl = case.attention(0, 0)
+    assert (np.abs(lse[0, rest] - el[rest]) <= tl[rest]).all() and (np.abs(o[0, rest] - eo[rest]) <= to[rest]).all()
+    case.check_attention(d.o, d.lse, rows=range(1, case.B * nq))
