@@ -563,7 +563,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
                         if (d != 0.0f) atomicOr(&S.moved[h >> 5], 1u << (h & 31));
                     }
                 }
-                seen = seen || mx[0] > -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 8; i++) seen = seen || mx[i] > -INFINITY;          // (a NaN head's are all -inf)
                 if (!first) {
                     tc::named_bar_sync(1, DA_STHREADS);
 #pragma unroll 1

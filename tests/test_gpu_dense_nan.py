@@ -56,3 +56,27 @@ def test_a_poisoned_head_is_nan_and_the_others_are_right(lens, nq, bad):
     eo, el, to, tl = case.attention(0, 0)
     assert (np.abs(lse[0, rest] - el[rest]) <= tl[rest]).all() and (np.abs(o[0, rest] - eo[rest]) <= to[rest]).all()
     case.check_attention(d.o, d.lse, rows=range(1, case.B * nq))
+
+
+def test_falling_logits_beside_a_poisoned_head():
+    """Head 0 of a query is NaN; head 1's logits fall from 0 to -400 over the sequence."""
+    import oracle
+    case = DenseCase(84, [128 * 6], window=False)
+    x = np.zeros((768, 512))
+    x[:, :256] = -np.repeat(np.arange(6) / 4.0, 128)[:, None]                  # 0, -0.25, ... as FP4 holds them
+    x[:, 256:] = case.rng.integers(1, 4, (768, 256))
+    codes, scales = oracle.KV_FORMATS[0][0](x.astype(np.float32))
+    at = case.slots(0, np.arange(768))
+    case.kv_codes[at], case.kv_scales[at] = codes, scales
+    q = np.zeros((200, 64, 512), np.float32)
+    q[:, :, :256] = 320 / 256
+    case.q, case.nq, case.B = q, 200, 1
+    case.q_pos = np.full((1, 200), 767)
+    case.q_bits = (q.view(np.uint32) >> 16).astype(np.uint16)
+    d = case.cuda()
+    d.q[:, 0, 3] = float("nan")
+    csa2.csa2_dense_attn(d.cache, d.batch, d.q, 1.0, d.o, d.lse)
+    o, lse = d.o.float().cpu().numpy(), d.lse.cpu().numpy()
+    eo, el, to, tl = case.attention(0, 0)
+    assert np.isnan(lse[:, 0]).all() and np.isnan(o[:, 0]).all()
+    assert (np.abs(lse[:, 1:] - el[1:]) <= tl[1:]).all() and (np.abs(o[:, 1:] - eo[1:]) <= to[1:]).all()
