@@ -59,7 +59,7 @@ def test_scales_far_apart(low, high):
     # (a single entry is its own output; 2.0 x 2^127 lies beyond fp32 and bf16)
     one = np.where(np.abs(case.keys[0]) < 2.0 ** 128, case.keys[0], np.sign(case.keys[0]) * np.inf)
     finite = np.isfinite(one)
-    assert (np.abs(o[1] - one)[:, finite] <= 2.0 ** -8 * np.abs(one[finite])).all()
+    assert (np.abs(o[1][:, finite] - one[finite]) <= 2.0 ** -8 * np.abs(one[finite])).all()
     assert (o[1][:, ~finite] == one[~finite]).all()
 
 
@@ -83,3 +83,46 @@ def test_one_entry_above_a_long_rest(B, n, nats):
     case = LongCase(codes_of(nib), np.full((65 * 64, 16), 127, np.uint8), table, [n] * B, bf16_values(q))
     d = case.cuda()
     case.check(d, [0, B // 2, B - 1], 32 * 17 * 2.0 ** -23 * 1.2 * nats)
+
+
+@pytest.mark.parametrize("nq,selected,fmt", [(1, False, 0), (1, False, 1), (2, False, 0), (1, True, 0), (4, True, 1)])
+def test_weights_of_a_million_entries(nq, selected, fmt):
+    """Three sequences of up to 1,048,576 entries; every entry's weight, or those of 512 a row up to the last."""
+    from compressed_sparse_attention_layer_gb300 import csa2
+    rng = np.random.default_rng(nq + fmt)
+    lens, P = [1 << 20, (1 << 20) - 37, 70], 1 << 14
+    nib = rng.integers(0, 16, (48 * 64, 512))
+    scales = rng.integers(0x30, 0x3c, (48 * 64, 32)) if fmt else rng.integers(125, 128, (48 * 64, 16))
+    case = LongCase(codes_of(nib), scales.astype(np.uint8), repeated_pages(3, P, 48), lens, queries(rng, 3, 1.0), fmt)
+    d = case.cuda()
+    q = torch.from_numpy(queries(rng, 3 * nq, 1.0)).cuda().to(torch.bfloat16)
+    pos = torch.tensor([n - 1 for n in lens for _ in range(nq)], device="cuda")
+    batch = csa2.batch_struct(d.n, pos, nq, 1, 1 << 20)
+    k = torch.from_numpy(case.keys).cuda()
+    l = q.double().view(3, nq * HEADS, 512) @ k.T                              # of the distinct entries
+    lse = (torch.logsumexp(l + torch.log(torch.from_numpy(np.stack([case.times(b) for b in range(3)])).cuda())[:, None], 2)
+           .view(3 * nq, HEADS).float())
+    idx = None
+    w = torch.exp(l.view(3, nq, HEADS, -1) - lse.double().view(3, nq, HEADS, 1)).sum(2)        # [3][nq][distinct]
+    at = (d.table.long()[:, :, None] * 64 + torch.arange(64, device="cuda")).view(3, -1)       # [3][2^20]
+    live = torch.arange(1 << 20, device="cuda") < d.n[:, None]
+    if selected:
+        idx = torch.full((3 * nq, 512), -1, dtype=torch.int32)
+        for r in range(3 * nq):
+            n = lens[r // nq]
+            e = np.unique(np.concatenate((rng.integers(0, n, 300), [0, n - 1])))
+            idx[r, :len(e)] = torch.from_numpy(e)
+        idx = idx.cuda()
+        want = torch.zeros((3, (1 << 20) + 1), dtype=torch.float64, device="cuda")
+        for r in range(3 * nq):
+            e = idx[r][idx[r] >= 0].long()
+            want[r // nq, e] += w[r // nq, r % nq][at[r // nq, e]]
+        want = want[:, :-1]
+    else:
+        want = torch.where(live, torch.gather(w.sum(1), 1, at), 0.0)
+    acc = torch.zeros((3, 1 << 20), device="cuda")
+    csa2.csa2_attn_weights(d.cache, batch, q, 1.0, lse, acc, idx=idx)
+    # logits of some units: 32 steps of 17 x 2^-23 of up to 4 each, l - lse rounded at 32, the exponential, 64 adds
+    tol = want * (32 * 17 * 2.0 ** -23 * 4 + 2.0 ** -18) + nq * 2.0 ** -40
+    assert bool(((acc.double() - want).abs() <= tol).all()) and bool((acc[~live] == 0).all())
+    assert int(d.status) == 0
