@@ -396,7 +396,9 @@ def csa2_evict(src: Cache, dst: Cache, n_entries, acc, max_entries: int, keep: i
                first: int = 0, recent: int = 0, evicted=None, evicted_out=None, stream=None):
     """Keeps min(n, keep) entries of each sequence of src -- the first `first`, the last `recent` and the
     largest acc (fp32 [B][ld]) -- and copies them to dst's pages.  kept int32 [B][keep], n_out int64 [B],
-    acc_out fp32 [B][ld_out] or None, evicted / evicted_out int64 [B] or None."""
+    acc_out fp32 [B][ld_out] or None, evicted / evicted_out int64 [B] or None.  csa2_dense_attn and
+    csa2_attn_weights take `evicted` from then on; csa2_layer, csa2_sparse_attn and the index calls cannot, and are
+    right for one query a sequence at its last token only, without ATTN_DEDUP_WINDOW."""
     B = n_entries.numel()
     if acc.dim() != 2 or acc.shape[0] != B or tuple(kept.shape) != (B, keep) or n_out.numel() != B or \
             (acc_out is not None and (acc_out.dim() != 2 or acc_out.shape[0] != B)) or \

@@ -481,7 +481,10 @@ CSA2_API size_t csa2_dense_attn_workspace_size(const csa2_batch *batch);
  *   k        0 when idx is NULL (CSA2_ERR_SHAPE otherwise)
  *   evicted  as the attention had it (NULL for csa2_sparse_attn and csa2_layer)
  *   swa      the attention's window, or NULL: with CSA2_ATTN_DEDUP_WINDOW the
- *            entries it left out get nothing; codes, flags and start are read
+ *            entries it left out get nothing; codes, flags and start are read.
+ *            As for csa2_dense_attn: new_rows NULL and flags at most
+ *            CSA2_ATTN_DEDUP_WINDOW, without evicted (CSA2_ERR_UNSUPPORTED) -- a
+ *            csa2_sparse_attn call's struct less its new_rows and other flags
  *   q        bf16 [B*Q][64][512], 16-byte aligned;  lse fp32 [B*Q][64]
  *   acc      fp32 [B][ld], ld >= batch->max_entries; entries no query saw keep
  *            their bits
@@ -491,7 +494,7 @@ CSA2_API size_t csa2_dense_attn_workspace_size(const csa2_batch *batch);
  * as by csa2_dense_attn; exponentials and sums are fp32.
  * The same inputs give the same bits: an entry's sum is taken in a fixed order,
  * over the rows of a selecting call with nq > 1 in 64-bit fixed point (steps of
- * 2^-40, a row's weight of an entry taken as at most 64).  A NaN makes the entries
+ * 2^-40, a row's weight of an entry taken as at most 64, their sum below 2^24).  A NaN makes the entries
  * that its query gives weight to NaN. */
 CSA2_API int csa2_attn_weights(const csa2_cache *cache, const csa2_batch *batch, const int64_t *evicted,
                                const uint16_t *q, float sm_scale, const int32_t *idx, int32_t k, const csa2_swa *swa,
@@ -499,13 +502,15 @@ CSA2_API int csa2_attn_weights(const csa2_cache *cache, const csa2_batch *batch,
                                csa2_stream_t stream);
 
 /* 0 for nq = 1.  Several queries: B * max_entries * 8 bytes with a selection
- * (k >= 1); without (k = 0) 64.5 KB a query, and at most 1.3 MB. */
+ * (k >= 1); without (k = 0) 64.5 KB a query, and at most 1.3 MB: calls that each take
+ * some of a long prompt's queries need less, and acc adds up. */
 CSA2_API size_t csa2_attn_weights_workspace_size(const csa2_batch *batch, int32_t k);
 
 /* ---- eviction by accumulated weight ------------------------------------------------
  * Of each sequence's n = n_entries[b] entries min(n, keep) stay: the first
  * `first` and the last `recent`, and of the rest those with the largest
- * acc[b][e] (ties -> lower index; -0.0 and +0.0 are equal).  They are copied in
+ * acc[b][e] (ties -> lower index; -0.0 and +0.0 are equal; a NaN is above every
+ * number, one with its sign set below).  They are copied in
  * ascending order to entries 0, 1, ... of the same sequence in dst: main KV and
  * its scales, and the indexer keys where src has them.
  *   src, dst caches of the same kv_format with their own block tables.  They may
@@ -525,8 +530,13 @@ CSA2_API size_t csa2_attn_weights_workspace_size(const csa2_batch *batch, int32_
  *   evicted_out  int64 [B] or NULL: evicted + n - n_out; may be evicted
  * An entry whose source or destination page id is outside its cache is not
  * copied and flags CSA2_DEV_BAD_PAGE in that cache's status.  A compacted
- * sequence is for decoding on: its entries are no longer one per token group,
- * so calls with causal queries inside it need `evicted`. */
+ * sequence is for decoding on: its entries are no longer one per token group, and
+ * which of them a query sees follows from `evicted`.  csa2_dense_attn and
+ * csa2_attn_weights take it.  csa2_layer, csa2_sparse_attn and the csa2_index calls do
+ * not, and cannot tell: after an eviction they see (t + 1) / m entries or all that there
+ * are, which is right for one query a sequence at its last token.  With several
+ * queries the earlier ones would see the later ones' entries, and
+ * CSA2_ATTN_DEDUP_WINDOW would take entry j for token j: neither may be used there. */
 CSA2_API int csa2_evict(const csa2_cache *src, const csa2_cache *dst, int32_t batch, int64_t max_entries,
                         const int64_t *n_entries, const float *acc, int64_t ld, int64_t keep, int64_t first,
                         int64_t recent, int32_t *kept, int64_t *n_out, float *acc_out, int64_t ld_out,

@@ -80,3 +80,24 @@ def test_falling_logits_beside_a_poisoned_head():
     eo, el, to, tl = case.attention(0, 0)
     assert np.isnan(lse[:, 0]).all() and np.isnan(o[:, 0]).all()
     assert (np.abs(lse[:, 1:] - el[1:]) <= tl[1:]).all() and (np.abs(o[:, 1:] - eo[1:]) <= to[1:]).all()
+
+
+def test_eviction_by_weights_that_are_not_numbers():
+    """A NaN is above +inf, one with its sign set below -inf; ties go to the lower index."""
+    case = DenseCase(85, [400], window=False)
+    d = case.cuda()
+    acc = case.rng.standard_normal((1, 400)).astype(np.float32)
+    acc[0, [10, 399, 77]] = np.nan
+    acc[0, [11, 200]] = np.inf
+    acc[0, [12, 300]] = -np.inf
+    bits = acc.view(np.uint32)
+    bits[0, [13, 14]] = 0xFFC00000
+    key = np.where(bits[0] >> 31, ~bits[0], bits[0] | 0x80000000)
+    for keep in (1, 3, 4, 5, 100, 395, 396, 397, 398, 399):
+        kept = torch.empty((1, keep), dtype=torch.int32, device="cuda")
+        n_out = torch.empty(1, dtype=torch.int64, device="cuda")
+        dst = [torch.zeros((448, 256), dtype=torch.uint8, device="cuda"), torch.zeros((448, 16), dtype=torch.uint8, device="cuda")]
+        table = torch.arange(7, dtype=torch.int32, device="cuda")[None].contiguous()
+        csa2.csa2_evict(d.cache, csa2.cache_struct(dst[0], dst[1], table), d.n, torch.from_numpy(acc).cuda(), 400, keep, kept, n_out)
+        order = sorted(range(400), key=lambda e: (-int(key[e]), e))[:keep]
+        assert kept.cpu().numpy()[0].tolist() == sorted(order) and int(n_out) == keep
