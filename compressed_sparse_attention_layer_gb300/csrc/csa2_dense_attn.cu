@@ -259,7 +259,7 @@ __device__ __forceinline__ void dense_window_part(const csa2_swa &swa, const Den
 // logits over a part begin when it is there, so keys, logits and the value product
 // of neighbouring tiles run side by side and only the softmax stands alone.
 //
-// 64 rows of 32,768 entries: 400 us (floor 145), 7,150 cycles a tile and SM.  The
+// 64 rows of 32,768 entries: 408 us (floor 145), 7,300 cycles a tile and SM.  The
 // products are 3,072 of them (32 + 32 instructions of M = 128, N = 64, 6 KB of shared
 // memory each at 126 of its 128 B a cycle); the keys' conversion, which the logits
 // wait for part by part, takes 2,400, the softmax 1,800, and moves of the reference
@@ -547,8 +547,8 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
                 for (int i = 0; i < 8; i++) {
                     const int h = hd + 8 * (i >> 1) + (i & 1);
                     const float m = fmaxf(fmaxf(S.red[0][h], S.red[1][h]), fmaxf(S.red[2][h], S.red[3][h]));
-                    // (with the head that passed move all that have come near: 400 us, with
-                    // those above 2^7.5 alone 409, for there are fewer moves to come)
+                    // (with the head that passed move all that have come near: 9 us less for 64
+                    // x 32,768 than with those above 2^7.5 alone, for there are fewer moves to come)
                     const float start = seen && at >= DA_FOLD ? DA_LATE : DA_START;
                     const bool up = seen ? m > start + 1.5f : m > -INFINITY;
                     const float d = up ? ceilf(m) - start : 0.0f;
