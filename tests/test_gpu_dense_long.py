@@ -126,3 +126,46 @@ def test_weights_of_a_million_entries(nq, selected, fmt):
     tol = want * (32 * 17 * 2.0 ** -23 * 4 + 2.0 ** -18) + nq * 2.0 ** -40
     assert bool(((acc.double() - want).abs() <= tol).all()) and bool((acc[~live] == 0).all())
     assert int(d.status) == 0
+
+
+@pytest.mark.parametrize("B,fmt", [(152, 0), (100, 1), (190, 0)])
+def test_long_rows_repeat_from_any_workspace(B, fmt):
+    """Outputs put by on the way through a row, whole or cut: the same bits from a workspace full of NaN, on
+    another stream and from a replayed graph."""
+    from compressed_sparse_attention_layer_gb300 import csa2
+    rng = np.random.default_rng(B)
+    nib = rng.integers(0, 16, (64 * 64, 512))
+    scales = rng.integers(0x30, 0x3c, (64 * 64, 32)) if fmt else rng.integers(124, 128, (64 * 64, 16))
+    lens = [40000 - 61 * (b % 9) for b in range(B)]
+    case = LongCase(codes_of(nib), scales.astype(np.uint8), repeated_pages(B, 625, 64), lens, queries(rng, B, 2.0), fmt)
+    d = case.cuda()
+    # logits of up to some ten units: 32 steps of 17 x 2^-23 of them, in a weight and in the sum
+    case.check(d, [0, 1, B // 2, B - 1], 32 * 17 * 2.0 ** -23 * 10)
+    first = d.o.clone(), d.lse.clone()
+    ws = torch.empty(csa2.csa2_dense_attn_workspace_size(d.batch), dtype=torch.uint8, device="cuda")
+
+    def call(stream=None):
+        csa2.csa2_dense_attn(d.cache, d.batch, d.q, 1.0, d.o, d.lse, workspace=ws, stream=stream)
+
+    def same():
+        torch.cuda.synchronize()
+        assert torch.equal(d.o.view(torch.int16), first[0].view(torch.int16)) and torch.equal(d.lse, first[1])
+        d.o.fill_(float("nan"))
+        d.lse.fill_(float("nan"))
+
+    for fill in (0xFF, 0x7F, 0):
+        ws.fill_(fill)
+        call()
+        same()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        call()
+    for _ in range(3):
+        ws.fill_(0xFF)
+        g.replay()
+        same()
+    call(side)
+    same()
+    assert int(d.status) == 0
