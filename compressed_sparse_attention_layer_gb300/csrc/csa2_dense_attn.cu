@@ -260,7 +260,7 @@ __device__ __forceinline__ void dense_window_part(const csa2_swa &swa, const Den
 // of neighbouring tiles run side by side and only the softmax stands alone.
 //
 // 64 rows of 32,768 entries: 408 us (floor 145), 7,300 cycles a tile and SM.  The
-// products are 3,072 of them (32 + 32 instructions of M = 128, N = 64, 6 KB of shared
+// products are 3,070 of them (32 + 32 instructions of M = 128, N = 64, 6 KB of shared
 // memory each at 126 of its 128 B a cycle); the keys' conversion, which the logits
 // wait for part by part, takes 2,400, the softmax 1,800, and moves of the reference
 // 700 (7,800 cycles each, one in eleven tiles with these logits).  Tiles of 64 keys, two
@@ -555,7 +555,9 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
                     const float f = exp2_approx(fminf(-d, 120.0f));             // (more only for sums of nothing)
                     mx[i] = m;
                     mu[i] += d;
-                    if (!first) l[i] *= f;
+                    // (in two steps: a sum of small scales may be 2^93 where 2^-d is 2^-195)
+                    const float d1 = truncf(0.5f * d);
+                    if (!first) l[i] = l[i] * exp2_approx(fminf(-d1, 60.0f)) * exp2_approx(fminf(d1 - d, 60.0f));
 #pragma unroll
                     for (int u = 0; u < 4; u++) x[16 * (u >> 1) + 4 * (i >> 1) + 2 * (u & 1) + (i & 1)] -= d;
                     if (quarter == 0 && lane < 4) {
@@ -715,9 +717,10 @@ __global__ void __launch_bounds__(DM_THREADS)
         const float base = M == -INFINITY ? 0.0f : M;
         float L = 0.0f;
         for (int i = lane; i < parts; i += 32) {
-            const float w = exp2f(wgt[i][j] - base);
-            wgt[i][j] = w;
-            L = fmaf(w, sum[i][j], L);
+            // (in two steps, as the references move in k_dense_attn)
+            const float d = wgt[i][j] - base, d1 = fmaxf(truncf(0.5f * d), -200.0f), w1 = exp2f(d1), w2 = exp2f(d - d1);
+            wgt[i][j] = w1 * w2;
+            L = fmaf(w1 * sum[i][j], w2, L);
         }
 #pragma unroll
         for (int w = 1; w < 32; w <<= 1) L += __shfl_xor_sync(0xffffffffu, L, w);

@@ -169,3 +169,25 @@ def test_long_rows_repeat_from_any_workspace(B, fmt):
     call(side)
     same()
     assert int(d.status) == 0
+
+
+@pytest.mark.parametrize("B,n", [(1, 256), (160, 384), (1, 30000), (3, 40001), (152, 20000)])
+@pytest.mark.parametrize("low,high,zeros", [(0, 0, True), (-66, 127, False), (0, 127, True), (-40, 100, True), (-90, 64, True)])
+def test_scales_far_apart_from_tile_to_tile(B, n, low, high, zeros):
+    """A query of zeros over a row whose first half is of one scale (or of zeros) and whose second is of another:
+    the reference moves by up to 195 from one tile or one part of the row to the next.  lse = log n all the same."""
+    rng = np.random.default_rng(n + high)
+    nib = rng.integers(1, 4, (4 * 64, 512))
+    scales = np.full((4 * 64, 16), 127 + low, np.uint8)
+    scales[128:] = 127 + high
+    if zeros:
+        nib[:64] = 0
+    pages = (n + 63) // 64
+    half = pages // 2
+    table = np.concatenate((np.arange(half) % (1 if zeros else 2), 2 + np.arange(pages - half) % 2))[None].repeat(B, 0)
+    case = LongCase(codes_of(nib), scales, table, [n] * B, np.zeros((B, HEADS, 512), np.float32))
+    d = case.cuda()
+    # as in test_scales_far_apart, the references of two parts; equal terms add up exactly
+    assert np.abs(d.lse.cpu().numpy() - np.log(n)).max() <= 2.0 ** -15
+    o, e = d.o[B // 2].float().cpu().numpy().astype(np.float64), case.attention(B // 2)[0]
+    assert (np.abs(o - e) <= 2.0 ** -8 * np.abs(e) + 2.0 ** -11 * np.abs(case.keys[128:]).max()).all()
