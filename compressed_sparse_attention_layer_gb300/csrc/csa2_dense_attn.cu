@@ -32,7 +32,8 @@ static_assert(DN_KWARPS * DA_REGS + DA_SWARPS * DA_REGS_SOFTMAX + 4 * DA_REGS_IS
 // The weights of the value product are held between 2^DA_START (the largest, when
 // the reference is set) and 2^DA_PASS (when it has to move), inside f16's range.  One
 // below 2^-25 adds nothing to the output, while the sum has it: up to 2^-24 of the
-// largest for each entry.  A long rest far below one entry must not go missing like
+// largest for each entry (2^-23 of a window row's, whose scale's mantissa is in its
+// weight).  A long rest far below one entry must not go missing like
 // that, so when a segment has had DA_FOLD tiles its references go down by up to 8, and a
 // later move ends at DA_LATE: n entries lose at most min(n, 16384) 2^-24 + n 2^-32 of the
 // largest, 2^-9.7 for a million.  (Without it 2.5 % of the mass were missing behind a first

@@ -458,7 +458,7 @@ CSA2_API int csa2_sparse_attn_schedule(const csa2_batch *batch, const csa2_swa *
  * two per key (its largest block scale) and per head: of one whose product with its
  * key's scale is below 2^-24 of the largest nothing may reach o, 2^-32 behind the
  * first 16,384 entries of a run, so n entries lose at most min(n, 16384) 2^-24 +
- * n 2^-32 of the largest; the sum takes every weight in fp32.  A page id outside the
+ * n 2^-32 of the largest (twice that of a window row's); the sum takes every weight in fp32.  A page id outside the
  * cache holds no keys (CSA2_DEV_BAD_PAGE).  A head whose logits are NaN has NaN in o
  * and lse. */
 CSA2_API int csa2_dense_attn(const csa2_cache *cache, const csa2_batch *batch, const int64_t *evicted,

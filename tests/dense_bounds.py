@@ -61,7 +61,11 @@ class TightCase(DenseCase):
         size = p @ np.abs(k)
         tiles = n // 128 + 2
         some = (k != 0).any(1)
-        floor = 2.0 ** -24 * (p * (w * some)[None]).max(1)[:, None] * (np.abs(k) / w[:, None]).sum(0)[None]
+        # a weight is rounded at 2^-25 where the largest 2^(y - mu) is 2^-1 or more.  Key j's place in the product
+        # is |k_j| / w_j; a window row's |k_j| / (w_j f_j), its scale's mantissa f_j in [1/2, 1) being in the weight
+        inv = 1.0 / w
+        inv[len(w) - len(self.window_tokens(b, i)):] *= 2
+        floor = 2.0 ** -24 * (p * (w * some)[None]).max(1)[:, None] * (np.abs(k) * inv[:, None]).sum(0)[None]
         exact = np.abs(p @ k)
         inner = (p * (2.0 ** -11 + np.expm1(dl))) @ np.abs(k) + floor + \
             (tol_lse[:, None] + min(8 * tiles, 1024) * STEP / 2 + 2.0 ** -18) * size
