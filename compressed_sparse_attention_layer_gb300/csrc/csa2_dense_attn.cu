@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(DA_THREADS, 1)
                 sc[h] = dense_pack_scales<E4M3>(raw[h], lane);
                 bool zero;
                 xk[h] = dense_exponent<E4M3>(code[h], sc[h], &zero);
+                if (E4M3) zero = dense_zero_codes(code[h]);
                 if (entries && (lane & 3) == 0)
                     S.kv[b][key + 64 * h] = !there[h] ? make_float2(-INFINITY, 0.0f) : zero ? make_float2(DN_XZERO, 0.0f) : make_float2((float)xk[h], 1.0f);
             }

@@ -142,8 +142,21 @@ __device__ __forceinline__ int64_t dense_page_slot(const csa2_cache &c, int32_t 
     return -1;
 }
 
+// An entry with E4M3 scales is all zeros, told by its codes.  Called by the whole warp.
+__device__ __forceinline__ bool dense_zero_codes(const uint4 (&codes)[4])
+{
+    uint32_t any = 0;
+#pragma unroll
+    for (int mt = 0; mt < 4; mt++) any |= codes[mt].x | codes[mt].y | codes[mt].z | codes[mt].w;
+    any &= 0x77777777u;
+    if (__all_sync(0xffffffffu, any != 0)) return false;
+    any |= __shfl_xor_sync(0xffffffffu, any, 1);
+    any |= __shfl_xor_sync(0xffffffffu, any, 2);
+    return any == 0;
+}
+
 // The exponent Xk of a quad's entry, from its four lanes' blocks; *zero: the
-// entry is all zeros.
+// entry is all zeros (MXFP4).
 template <bool E4M3>
 __device__ __forceinline__ int dense_exponent(const uint4 (&codes)[4], uint2 scales, bool *zero)
 {

@@ -225,3 +225,27 @@ def test_weights_beside_garbage_that_no_query_sees(nq, fmt):
     got = acc.cpu().numpy()
     assert (np.abs(got - 0.25 - want) <= tol + 2.0 ** -23 * (0.25 + want)).all()
     assert (got[want == 0] == 0.25).all()
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("n", [2, 130, 3000])
+def test_heads_that_lean_on_a_key_of_zeros(n, fmt):
+    """The first entry is zeros and every other's logit is -14 to -40: what reaches o are the others' small
+    weights alone, and they keep their bits."""
+    case = TightCase(880 + n + fmt, [n, n], fmt=fmt, window=False, sink=n == 130)
+    rng = np.random.default_rng(n)
+    for b in range(2):
+        at = case.slots(b, np.arange(n))
+        nib = rng.integers(0, 16, (n, 512))
+        nib[:, :64] = 2                            # 1.0 where the query looks
+        nib[0] = 0
+        case.kv_codes[at] = codes_of(nib)
+        case.kv_scales[at] = 0x38 if fmt else 127
+    q = np.zeros((2, 64, 512), np.float32)
+    q[:, :, :64] = -np.linspace(14, 40, 64)[:, None] / 64
+    q[:, :, 64:] = 0.002 * rng.standard_normal((2, 64, 448))
+    case.q, case.q_bits = bf16(q)
+    d = case.cuda()
+    attend(d, case)
+    case.check_attention(d.o, d.lse)
+    assert int(d.status) == 0
